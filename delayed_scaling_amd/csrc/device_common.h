@@ -102,11 +102,13 @@ __device__ __forceinline__ v4i rsrc_words(const void* base, uint32_t bytes) {
 // at or past the buffer size lands as zeros.  Written as inline asm so the
 // compiler does not guard every later LDS read with a wait for all
 // outstanding loads: callers count these loads themselves (vmcnt) and order
-// LDS through barriers.  The instruction writes no VGPR.
+// LDS through barriers.  The instruction writes no VGPR.  The s_nop is the wait
+// state the load needs after the scalar write of m0, without which it may take
+// the LDS address of the load before it; nothing inserts it inside inline asm.
 __device__ __forceinline__ void load_lds16(v4i rsrc, uint32_t lds_base, uint32_t voff, uint32_t soff) {
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
                : "s"(lds_base), "v"(voff), "s"(rsrc), "s"(soff)
                : "memory", "m0");
@@ -117,7 +119,7 @@ __device__ __forceinline__ void load_lds16(v4i rsrc, uint32_t lds_base, uint32_t
 __device__ __forceinline__ void load_lds4(v4i rsrc, uint32_t lds_base, uint32_t voff) {
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
                :
                : "s"(lds_base), "v"(voff), "s"(rsrc)
                : "memory", "m0");
