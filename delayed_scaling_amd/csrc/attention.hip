@@ -190,12 +190,13 @@ __device__ __forceinline__ float dot8(v4i x, v4i y, float s) {
   return s;
 }
 
-// (fmaxf would first quieten each operand, twice the instructions.  A NaN loses
-// against a number here too; it comes back through the exponential.)
+// The larger of three.  (The builtins, which compile to one v_max3_f32, and not
+// that instruction as inline asm: its operands are results of matrix products,
+// and the compiler puts the wait states those need only before instructions it
+// knows.  A NaN loses against a number here; it comes back through the
+// exponential.)
 __device__ __forceinline__ float max3(float x, float y, float z) {
-  float r;
-  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(x), "v"(y), "v"(z));
-  return r;
+  return __builtin_fmaxf(__builtin_fmaxf(x, y), z);
 }
 
 // The value of the lane 32 away.

@@ -143,7 +143,7 @@ def test_the_code_is_read(found):
     assert found[1]["m0"] > 1000 and found[1]["product"] > 1000 and found[1]["functions"] > 100
 
 
-@pytest.mark.parametrize("kind", ["m0", "scalar register"])
+@pytest.mark.parametrize("kind", ["m0", "scalar register", "product"])
 def test_no_wait_is_missing(found, kind):
     bad = [x for x in found[0] if x[0] == kind]
     assert not bad, (len(bad), len({x[1] for x in bad}), bad[:3])
