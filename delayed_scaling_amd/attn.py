@@ -49,6 +49,13 @@ def _view(t, name, shape, dtype, device):
             st[2] if shape[2] > 1 else 0)
 
 
+def _int32(x):
+    """A length or window as the 32-bit integer of the arguments.  No row is as far
+    as the largest one, so a window past it hides as little, and lengths there
+    are refused by the library."""
+    return max(-1, min(int(x), 0x7FFFFFFF))
+
+
 def _tail(q, k, causal, window, scale, cu_q, cu_k, max_q, max_k):
     """The scalar fields of the arguments (after lse and workspace), and the
     shape of lse."""
@@ -67,7 +74,7 @@ def _tail(q, k, causal, window, scale, cu_q, cu_k, max_q, max_k):
     scale = dim ** -0.5 if scale is None else float(scale)
     if not packed:
         batch, tq = qs[0], qs[1]
-        return (0, 0, tq, tq, ks[1], _TYPES[q.dtype], batch, hq, hkv, dim, tq, ks[1], 1 if causal else 0, int(window),
+        return (0, 0, tq, tq, ks[1], _TYPES[q.dtype], batch, hq, hkv, dim, tq, ks[1], 1 if causal else 0, _int32(window),
                 scale), (batch, hq, tq)
     for name, cu in (("cu_seqlens_q", cu_q), ("cu_seqlens_k", cu_k)):
         _need(cu, name, (torch.int32,), 4)
@@ -78,7 +85,7 @@ def _tail(q, k, causal, window, scale, cu_q, cu_k, max_q, max_k):
     if max_q is None or max_k is None:
         raise Fp8dsError("cu_seqlens need max_seqlen_q and max_seqlen_k")
     return (cu_q.data_ptr(), cu_k.data_ptr(), qs[0], qs[0], ks[0], _TYPES[q.dtype], cu_q.shape[0] - 1, hq, hkv, dim,
-            int(max_q), int(max_k), 1 if causal else 0, int(window), scale), (hq, qs[0])
+            _int32(max_q), _int32(max_k), 1 if causal else 0, _int32(window), scale), (hq, qs[0])
 
 
 def _lse(t, shape, device):

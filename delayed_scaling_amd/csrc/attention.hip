@@ -709,7 +709,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_dkv_kernel(AttnArgs a) {
     hi = s.nq;
     const int last = min(k0 + n, s.nk) - 1;
     if (a.causal) lo = (int)max((int64_t)0, min((int64_t)s.nq, k0 - off));
-    if (a.window) hi = (int)max((int64_t)0, min((int64_t)s.nq, last + a.window - off));
+    if (a.window) hi = (int)max((int64_t)0, min((int64_t)s.nq, (int64_t)last + a.window - off));
   };
   int rlo, rhi, ilo, ihi;
   row_range(key0, kRows, rlo, rhi);

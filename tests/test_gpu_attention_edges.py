@@ -27,3 +27,20 @@ def test_a_maximum_in_the_middle_of_an_unmasked_tile(kind, d, at):
     torch.cuda.synchronize()
     assert (lse > 20).all()
     check_dense((q, k, v, do), o, lse, grads, kind, False, 0, None)
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 40, 2 ** 40])
+@pytest.mark.parametrize("tq,tk", [(300, 300), (200, 340), (1100, 600)])
+def test_a_window_past_every_row_hides_nothing(window, tq, tk):
+    """The largest windows (row numbers added to them leave 32 bits) give the bits
+    of no window; the last case's backward is shared by workgroups."""
+    ds = require_gpu()
+    say("attention window", window, tq, tk)
+    q, k, v, do = (randn((1, t, h, 64), 320 + i, "bf16") for i, (t, h) in enumerate(((tq, 4), (tk, 2), (tk, 2), (tq, 4))))
+    o, lse = ds.attn_forward(q, k, v, causal=True)
+    ref = ds.attn_backward(do, q, k, v, o, lse, causal=True)
+    o2, lse2 = ds.attn_forward(q, k, v, causal=True, window=window)
+    got = ds.attn_backward(do, q, k, v, o2, lse2, causal=True, window=window)
+    torch.cuda.synchronize()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert all(torch.equal(a, b) for a, b in zip(got, ref)) and (ref[1] != 0).any() and (ref[2] != 0).any()
