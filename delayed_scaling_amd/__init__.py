@@ -142,6 +142,8 @@ def lib():
         L.attn_workspace_bytes.argtypes = [vp]
         L.adamw_step.restype = i32
         L.adamw_step.argtypes = [vp, i32, vp, vp]
+        L.adamw_step_counts.restype = i32
+        L.adamw_step_counts.argtypes = [vp, vp, i32, vp, vp]
         L.adamw_state_values.restype = i32
         L.adamw_state_values.argtypes = [vp, vp, i64, i32, vp, vp]
         L.fp8_last_error.restype = ctypes.c_char_p

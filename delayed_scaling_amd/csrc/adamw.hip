@@ -54,6 +54,7 @@ struct AdamTensor {
   float* w;
   uint8_t* me;
   uint8_t* ve;
+  const int32_t* step;           // the device step count, or null
   uint32_t numel;
   uint32_t key;      // seed and tensor number, mixed on the host
 };
@@ -64,12 +65,12 @@ struct AdamArgs {
   float b1, b2, c1, c2;          // betas and 1 - betas
   float decay, step_size, inv_sqrt_bc2, eps;
   const float* grad_scale;
-  const float* lr_dev;           // with step_dev or lr_dev, decay, step_size and
-  const int32_t* step_dev;       // inv_sqrt_bc2 are formed in the kernel
+  const float* lr_dev;           // with it or a tensor's step, decay, step_size and
+                                 // inv_sqrt_bc2 are formed in the kernel
   float lr, wd, ln_b1, ln_b2;
   int32_t step;
-  uint32_t seed_dev;             // nonzero: *step_dev joins the keys
 };
+static_assert(sizeof(AdamArgs) <= 4096, "kernel arguments");
 
 // 32 random bits for element i: an add and two multiplications by odd numbers
 // (the fractions of the golden ratio and of the square roots of 2 and 3),
@@ -227,14 +228,14 @@ __global__ __launch_bounds__(kAThreads) void adamw_kernel(AdamArgs a) {
   const uint32_t n = t.numel;
   uint32_t key = t.key;
   float decay = a.decay, step_size = a.step_size, inv_sqrt_bc2 = a.inv_sqrt_bc2;
-  if (a.lr_dev || a.step_dev) {
+  if (a.lr_dev || t.step) {
     const float lr = a.lr_dev ? *a.lr_dev : a.lr;
-    const int32_t step = a.step_dev ? *a.step_dev : a.step;
+    const int32_t step = t.step ? *t.step : a.step;
     // 1 - b^t = -expm1(t ln b)
     decay = 1.0f - lr * a.wd;
     step_size = lr / -expm1f((float)step * a.ln_b1);
     inv_sqrt_bc2 = 1.0f / sqrtf(-expm1f((float)step * a.ln_b2));
-    if (a.seed_dev) key += (uint32_t)step * kRoot2;
+    if (t.step) key += (uint32_t)step * kRoot2;
   }
   const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
   const uintptr_t all = reinterpret_cast<uintptr_t>(t.p) | reinterpret_cast<uintptr_t>(t.g) |
@@ -350,7 +351,8 @@ AdamFn pick_grad(int gt, bool master, int bits) {
 
 }  // namespace
 
-int launch_adamw(const fp8ds_adamw_tensor* ts, int nt, const fp8ds_adamw_args& p, bool master, hipStream_t stream) {
+int launch_adamw(const fp8ds_adamw_tensor* ts, const int32_t* const* steps, int nt, const fp8ds_adamw_args& p,
+                 bool master, hipStream_t stream) {
   AdamFn fn = p.param_type == kInBf16  ? pick_grad<kInBf16>(p.grad_type, master, p.state_bits)
               : p.param_type == kInF16 ? pick_grad<kInF16>(p.grad_type, master, p.state_bits)
                                        : pick_grad<kInF32>(p.grad_type, master, p.state_bits);
@@ -367,14 +369,12 @@ int launch_adamw(const fp8ds_adamw_tensor* ts, int nt, const fp8ds_adamw_args& p
   a.step = (int32_t)p.step;
   a.decay = (float)(1.0 - p.lr * p.weight_decay);
   a.step_size = a.inv_sqrt_bc2 = 0.0f;
-  if (!p.step_dev) {
+  if (!p.step_dev && !steps) {
     a.step_size = (float)(p.lr / (1.0 - __builtin_pow(p.beta1, (double)p.step)));
     a.inv_sqrt_bc2 = (float)(1.0 / __builtin_sqrt(1.0 - __builtin_pow(p.beta2, (double)p.step)));
   }
   a.grad_scale = p.grad_scale;
   a.lr_dev = p.lr_dev;
-  a.step_dev = p.step_dev;
-  a.seed_dev = p.step_dev != nullptr;
   int at = 0;
   while (at < nt) {
     int used = 0;
@@ -385,7 +385,7 @@ int launch_adamw(const fp8ds_adamw_tensor* ts, int nt, const fp8ds_adamw_args& p
       const uint64_t need = ((uint64_t)s.numel + kTile * kTilesPerGroup - 1) / (kTile * kTilesPerGroup);
       if (groups + need > 0x7FFFFFFFu) break;
       a.t[used] = AdamTensor{s.p, s.g, s.exp_avg, s.exp_avg_sq, s.master, s.exp_avg_exp, s.exp_avg_sq_exp,
-                             (uint32_t)s.numel, p.seed ^ (uint32_t)at * kRoot3};
+                             steps ? steps[at] : p.step_dev, (uint32_t)s.numel, p.seed ^ (uint32_t)at * kRoot3};
       a.first[used] = (uint32_t)groups;
       groups += need;
       ++used;

@@ -92,6 +92,53 @@ int64_t view_extent(int64_t rows, int64_t cols, int64_t ld) {
   return (e + 15) & ~int64_t(15);
 }
 
+// Checks and launch of the AdamW entry points; steps: a device count for each tensor, or null.
+int adamw_call(const char* fn, const fp8ds_adamw_tensor* ts, const int32_t* const* steps, int nt,
+               const fp8ds_adamw_args* a, void* stream) {
+  if (!a) return set_error(FP8DS_EINVAL, "%s: args is NULL", fn);
+  if (nt < 0) return set_error(FP8DS_EINVAL, "%s: ntensors %d < 0", fn, nt);
+  if (nt > 0 && !ts) return set_error(FP8DS_EINVAL, "%s: tensors is NULL", fn);
+  if (!valid_in(a->param_type) || !valid_in(a->grad_type))
+    return set_error(FP8DS_EINVAL, "%s: param_type and grad_type are bf16 (0), fp16 (1) or fp32 (2)", fn);
+  if (a->state_bits != 8 && a->state_bits != 32)
+    return set_error(FP8DS_EUNSUPPORTED, "%s: state_bits %d is neither 8 nor 32", fn, a->state_bits);
+  if (!(a->beta1 >= 0 && a->beta1 < 1 && a->beta2 >= 0 && a->beta2 < 1))
+    return set_error(FP8DS_EINVAL, "%s: betas must be in [0, 1)", fn);
+  if (!(a->eps >= 0 && a->eps < __builtin_inf()) || !(a->weight_decay >= 0 && a->weight_decay < __builtin_inf()) ||
+      !(a->lr >= 0 && a->lr < __builtin_inf()))
+    return set_error(FP8DS_EINVAL, "%s: lr, eps and weight_decay must be finite and >= 0", fn);
+  if (!steps && !a->step_dev && (a->step < 1 || a->step > kMaxDim))
+    return set_error(FP8DS_EINVAL, "%s: step %lld outside [1, 2^31)", fn, (long long)a->step);
+  if (((reinterpret_cast<uintptr_t>(a->lr_dev) | reinterpret_cast<uintptr_t>(a->step_dev) |
+        reinterpret_cast<uintptr_t>(a->grad_scale)) & 3u) != 0)
+    return set_error(FP8DS_EALIGN, "%s: lr_dev, step_dev and grad_scale are 4-byte aligned", fn);
+  int masters = 0, live = 0;
+  for (int i = 0; i < nt; ++i) {
+    const fp8ds_adamw_tensor& t = ts[i];
+    if (t.numel < 0 || t.numel > 0xFFFFF000LL)
+      return set_error(FP8DS_EINVAL, "%s: tensor %d has %lld elements, outside [0, 2^32 - 4096]", fn, i, (long long)t.numel);
+    if (t.numel == 0) continue;
+    ++live;
+    masters += t.master != nullptr;
+    if (!t.p || !t.g || !t.exp_avg || !t.exp_avg_sq)
+      return set_error(FP8DS_EINVAL, "%s: tensor %d has a NULL pointer", fn, i);
+    if (steps && (!steps[i] || (reinterpret_cast<uintptr_t>(steps[i]) & 3u)))
+      return set_error(steps[i] ? FP8DS_EALIGN : FP8DS_EINVAL, "%s: the step count of tensor %d is NULL or not 4-byte aligned", fn, i);
+    if (a->state_bits == 8 && (!t.exp_avg_exp || !t.exp_avg_sq_exp))
+      return set_error(FP8DS_EINVAL, "%s: tensor %d has 8-bit states and no exponent bytes", fn, i);
+    const uintptr_t state = a->state_bits == 32 ? 3u : 0u;
+    if ((reinterpret_cast<uintptr_t>(t.p) & (uintptr_t)(in_size(a->param_type) - 1)) ||
+        (reinterpret_cast<uintptr_t>(t.g) & (uintptr_t)(in_size(a->grad_type) - 1)) ||
+        ((reinterpret_cast<uintptr_t>(t.exp_avg) | reinterpret_cast<uintptr_t>(t.exp_avg_sq)) & state) ||
+        (reinterpret_cast<uintptr_t>(t.master) & 3u))
+      return set_error(FP8DS_EALIGN, "%s: an array of tensor %d is not aligned to its elements", fn, i);
+  }
+  if (masters != 0 && masters != live)
+    return set_error(FP8DS_EINVAL, "%s: %d of %d tensors have a master copy; all or none may", fn, masters, live);
+  if (live == 0) return FP8DS_OK;
+  return launch_adamw(ts, steps, nt, *a, masters != 0, static_cast<hipStream_t>(stream));
+}
+
 }  // namespace
 }  // namespace fp8ds
 
@@ -489,47 +536,14 @@ int attn_backward(const fp8ds_attn_args* a, void* stream) {
 }
 
 int adamw_step(const fp8ds_adamw_tensor* ts, int nt, const fp8ds_adamw_args* a, void* stream) {
-  const char* fn = "adamw_step";
-  if (!a) return set_error(FP8DS_EINVAL, "%s: args is NULL", fn);
-  if (nt < 0) return set_error(FP8DS_EINVAL, "%s: ntensors %d < 0", fn, nt);
-  if (nt > 0 && !ts) return set_error(FP8DS_EINVAL, "%s: tensors is NULL", fn);
-  if (!valid_in(a->param_type) || !valid_in(a->grad_type))
-    return set_error(FP8DS_EINVAL, "%s: param_type and grad_type are bf16 (0), fp16 (1) or fp32 (2)", fn);
-  if (a->state_bits != 8 && a->state_bits != 32)
-    return set_error(FP8DS_EUNSUPPORTED, "%s: state_bits %d is neither 8 nor 32", fn, a->state_bits);
-  if (!(a->beta1 >= 0 && a->beta1 < 1 && a->beta2 >= 0 && a->beta2 < 1))
-    return set_error(FP8DS_EINVAL, "%s: betas must be in [0, 1)", fn);
-  if (!(a->eps >= 0 && a->eps < __builtin_inf()) || !(a->weight_decay >= 0 && a->weight_decay < __builtin_inf()) ||
-      !(a->lr >= 0 && a->lr < __builtin_inf()))
-    return set_error(FP8DS_EINVAL, "%s: lr, eps and weight_decay must be finite and >= 0", fn);
-  if (!a->step_dev && (a->step < 1 || a->step > kMaxDim))
-    return set_error(FP8DS_EINVAL, "%s: step %lld outside [1, 2^31)", fn, (long long)a->step);
-  if (((reinterpret_cast<uintptr_t>(a->lr_dev) | reinterpret_cast<uintptr_t>(a->step_dev) |
-        reinterpret_cast<uintptr_t>(a->grad_scale)) & 3u) != 0)
-    return set_error(FP8DS_EALIGN, "%s: lr_dev, step_dev and grad_scale are 4-byte aligned", fn);
-  int masters = 0, live = 0;
-  for (int i = 0; i < nt; ++i) {
-    const fp8ds_adamw_tensor& t = ts[i];
-    if (t.numel < 0 || t.numel > 0xFFFFF000LL)
-      return set_error(FP8DS_EINVAL, "%s: tensor %d has %lld elements, outside [0, 2^32 - 4096]", fn, i, (long long)t.numel);
-    if (t.numel == 0) continue;
-    ++live;
-    masters += t.master != nullptr;
-    if (!t.p || !t.g || !t.exp_avg || !t.exp_avg_sq)
-      return set_error(FP8DS_EINVAL, "%s: tensor %d has a NULL pointer", fn, i);
-    if (a->state_bits == 8 && (!t.exp_avg_exp || !t.exp_avg_sq_exp))
-      return set_error(FP8DS_EINVAL, "%s: tensor %d has 8-bit states and no exponent bytes", fn, i);
-    const uintptr_t state = a->state_bits == 32 ? 3u : 0u;
-    if ((reinterpret_cast<uintptr_t>(t.p) & (uintptr_t)(in_size(a->param_type) - 1)) ||
-        (reinterpret_cast<uintptr_t>(t.g) & (uintptr_t)(in_size(a->grad_type) - 1)) ||
-        ((reinterpret_cast<uintptr_t>(t.exp_avg) | reinterpret_cast<uintptr_t>(t.exp_avg_sq)) & state) ||
-        (reinterpret_cast<uintptr_t>(t.master) & 3u))
-      return set_error(FP8DS_EALIGN, "%s: an array of tensor %d is not aligned to its elements", fn, i);
-  }
-  if (masters != 0 && masters != live)
-    return set_error(FP8DS_EINVAL, "%s: %d of %d tensors have a master copy; all or none may", fn, masters, live);
-  if (live == 0) return FP8DS_OK;
-  return launch_adamw(ts, nt, *a, masters != 0, static_cast<hipStream_t>(stream));
+  return adamw_call("adamw_step", ts, nullptr, nt, a, stream);
+}
+
+int adamw_step_counts(const fp8ds_adamw_tensor* ts, const int32_t* const* steps, int nt, const fp8ds_adamw_args* a,
+                      void* stream) {
+  if (nt > 0 && !steps) return set_error(FP8DS_EINVAL, "adamw_step_counts: steps is NULL");
+  const int32_t* const none = nullptr;
+  return adamw_call("adamw_step_counts", ts, steps ? steps : &none, nt, a, stream);
 }
 
 int adamw_state_values(const uint8_t* codes, const uint8_t* exps, int64_t numel, int is_signed, void* out,

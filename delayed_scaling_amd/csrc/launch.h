@@ -73,8 +73,9 @@ int gemm_pair_tile(const GemmProblem& p0, const GemmProblem& p1);
 int launch_attn_forward(const fp8ds_attn_args& args, hipStream_t stream);
 int launch_attn_backward(const fp8ds_attn_args& args, hipStream_t stream);
 size_t attn_backward_workspace(const fp8ds_attn_args& args);
-int launch_adamw(const fp8ds_adamw_tensor* tensors, int ntensors, const fp8ds_adamw_args& args, bool master,
-                 hipStream_t stream);
+// steps: a device step count for each tensor, or null (args.step or args.step_dev, for all).
+int launch_adamw(const fp8ds_adamw_tensor* tensors, const int32_t* const* steps, int ntensors,
+                 const fp8ds_adamw_args& args, bool master, hipStream_t stream);
 int launch_adamw_state_values(const uint8_t* codes, const uint8_t* exps, int64_t numel, bool is_signed, void* out,
                               hipStream_t stream);
 

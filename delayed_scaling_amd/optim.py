@@ -74,7 +74,8 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, *, step, lr, betas=(0.9, 0.99
     masters: fp32 copies the step is taken on (the parameters then receive
     their rounded values).  step (t >= 1) and lr: numbers, or device scalars
     (int32 and fp32 tensors) read when the kernel runs, so that a captured
-    graph can be replayed with new ones.  grad_scale: optional fp32 device
+    graph can be replayed with new ones; step may also be a list of them, one
+    for each parameter.  grad_scale: optional fp32 device
     scalar that multiplies every gradient.  seed: of the 8-bit states'
     stochastic rounding; pass another every step (a device step joins it)."""
     n = len(params)
@@ -98,13 +99,22 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, *, step, lr, betas=(0.9, 0.99
                _addresses("exp_avg_exp", exp_avg_exp, numels, torch.uint8, dev, exps),
                _addresses("exp_avg_sq_exp", exp_avg_sq_exp, numels, torch.uint8, dev, exps), numels)
     table = b"".join([_ADAM_TENSOR.pack(*c) for c in cols])
+    steps = None
+    if isinstance(step, (list, tuple)):
+        if len(step) != n:
+            raise Fp8dsError(f"step has {len(step)} tensors; params has {n}")
+        steps = struct.pack(f"<{n}Q", *[_scalar(t, f"step[{i}]", torch.int32, dev) for i, t in enumerate(step)])
+        step = 1                             # (not used)
     step_dev = _scalar(step, "step", torch.int32, dev) if isinstance(step, torch.Tensor) else 0
     lr_dev = _scalar(lr, "lr", _F32, dev) if isinstance(lr, torch.Tensor) else 0
     gs = 0 if grad_scale is None else _scalar(grad_scale, "grad_scale", _F32, dev)
     args = _ADAM_ARGS.pack(0.0 if lr_dev else float(lr), float(betas[0]), float(betas[1]), float(eps),
                            float(weight_decay), 1 if step_dev else int(step), lr_dev, step_dev, gs,
                            _IN_TYPE[p0.dtype], _IN_TYPE[g0.dtype], bits, int(seed) & 0xFFFFFFFF)
-    _check(lib().adamw_step(table, n, args, _stream(stream)))
+    if steps is None:
+        _check(lib().adamw_step(table, n, args, _stream(stream)))
+    else:
+        _check(lib().adamw_step_counts(table, steps, n, args, _stream(stream)))
 
 
 def adamw_state_values(codes, exps, signed, out=None, stream=None):
@@ -128,7 +138,7 @@ class AdamW(torch.optim.Optimizer):
 
     state_bits 8 keeps both moments in 8 bits (2 bytes a parameter instead of
     8); master_weights keeps an fp32 copy of bf16 / fp16 parameters, on which
-    the step is taken.  capturable: the step count (and with lr a tensor, the
+    the step is taken.  capturable: the step counts (and with lr a tensor, the
     rate) live on the device, so a captured step can be replayed.  seed: of the
     8-bit states' rounding."""
 
@@ -189,7 +199,8 @@ class AdamW(torch.optim.Optimizer):
                 with torch.cuda.device(key[0]):
                     adamw_step([p.detach() for p in ps],
                                [p.grad if p.grad.is_contiguous() else p.grad.contiguous() for p in ps],
-                               [s["exp_avg"] for s in ss], [s["exp_avg_sq"] for s in ss], step=ss[0]["step"],
+                               [s["exp_avg"] for s in ss], [s["exp_avg_sq"] for s in ss],
+                               step=[s["step"] for s in ss] if self.capturable else ss[0]["step"],
                                lr=group["lr"], betas=group["betas"], eps=group["eps"],
                                weight_decay=group["weight_decay"],
                                masters=[s["master"] for s in ss] if "master" in ss[0] else None,

@@ -454,6 +454,11 @@ typedef struct fp8ds_adamw_args {
   uint32_t seed;            /* 8-bit states                                       */
 } fp8ds_adamw_args;
 int adamw_step(const fp8ds_adamw_tensor* tensors, int ntensors, const fp8ds_adamw_args* args, void* stream);
+/* The same with a step count for each tensor: steps: host array of ntensors
+ * device pointers, read by the kernel as step_dev is (args' step and step_dev
+ * are unused).  For tensors that have not all taken part in every step. */
+int adamw_step_counts(const fp8ds_adamw_tensor* tensors, const int32_t* const* steps, int ntensors,
+                      const fp8ds_adamw_args* args, void* stream);
 
 /* The values 8-bit state codes stand for, as bf16 (which holds them exactly):
  * codes: device uint8[numel]; exps: device uint8[ceil(numel / 256)];
