@@ -170,6 +170,10 @@ class AdamW(torch.optim.Optimizer):
         for i, p in zip(ids, (p for g in self.param_groups for p in g["params"])):
             for key, value in state_dict["state"].get(i, {}).items():
                 self.state[p][key] = value.detach().to(p.device).clone() if isinstance(value, torch.Tensor) else value
+            count = self.state.get(p, {}).get("step")    # of the other kind, if such an optimizer saved it
+            if count is not None and isinstance(count, torch.Tensor) != self.capturable:
+                self.state[p]["step"] = int(count) if not self.capturable else \
+                    torch.tensor(count, dtype=torch.int32, device=p.device)
 
     @torch.no_grad()
     def step(self, closure=None, grad_scale=None):

@@ -144,3 +144,31 @@ def test_half_precision_parameters_resume(bits, capturable):
     torch.cuda.synchronize()
     for p, q in zip(mine, again):
         assert torch.equal(p, q) and torch.equal(opt.state[p]["master"], opt2.state[q]["master"])
+
+
+@pytest.mark.parametrize("capturable", [False, True])
+def test_a_state_of_the_other_kind_resumes(capturable):
+    """A state saved with counts on the host goes on with counts on the device, and
+    the other way round, as if it had been of that kind all along (the bias
+    corrections of device counts are fp32: `close`)."""
+    ds = require_gpu()
+    torch.manual_seed(4)
+    mine = [torch.nn.Parameter(torch.randn(s, device="cuda")) for s in SHAPES]
+
+    def run(opt, ps, ts):
+        for t in ts:
+            for p, g in zip(ps, grads(t, SHAPES)):
+                p.grad = g
+            opt.step()
+
+    opt = ds.AdamW(mine, lr=LR, weight_decay=WD, capturable=not capturable)
+    run(opt, mine, range(4))
+    again = [torch.nn.Parameter(p.detach().clone()) for p in mine]
+    opt2 = ds.AdamW(again, lr=LR, weight_decay=WD, capturable=capturable)
+    opt2.load_state_dict(copy.deepcopy(opt.state_dict()))
+    assert all(isinstance(opt2.state[p]["step"], torch.Tensor) == capturable for p in again)
+    run(opt, mine, range(4, 8))
+    run(opt2, again, range(4, 8))
+    torch.cuda.synchronize()
+    close(mine, again, 4)
+    assert all(int(opt2.state[p]["step"]) == 8 for p in again)
