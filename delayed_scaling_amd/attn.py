@@ -13,6 +13,7 @@ holds the formulas and the masks.
 import struct
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _F32, IN_BF16, IN_F16, Fp8dsError, _check, _need, _stream, lib
 
@@ -159,6 +160,7 @@ class _AttentionFn(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable   # (its outputs are written through addresses: no graph leads on)
     def backward(ctx, dout):
         q, k, v, out, lse = ctx.saved_tensors
         if dout.dtype != q.dtype or dout.stride(-1) != 1 or dout.data_ptr() % 16 or any(s % 8 for s in dout.stride()[:-1]):

@@ -21,6 +21,7 @@ the size the call needs, so the per-tensor checks of the general binding
 (which cost more host time than the launches) reduce to those four tensors.
 """
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (_IN_TYPE, _MMARGS, _QJOB, BIAS_BF16, BIAS_F32, BIAS_NONE, E4M3, E5M2, G_BF16, NN, NT, TN,
                BiasGradWorkspace, Fp8dsError, ScaleRing, _check, _stream, bias_grad_workspace_bytes, lib)
@@ -116,6 +117,7 @@ class _Fp8LinearFn(torch.autograd.Function):
         return y.view(*x.shape[:-1], n_out)
 
     @staticmethod
+    @once_differentiable   # (its outputs are written through addresses: no graph leads on)
     def backward(ctx, gy):
         saved, = ctx.saved_tensors
         t, n_in, n_out = ctx.dims

@@ -12,6 +12,7 @@ of its own; the backward multiplies the forward's codes and dequantizes with the
 1/scale values the forward applied, as the linear layer does.
 """
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU, E4M3, E5M2, NN, NT, TN, BiasGradWorkspace,
                Fp8dsError, ScaleRing, bias_grad_workspace_bytes, fp8_bias_grad, fp8_mm, fp8_mm_epilogue, fp8_mm_pair,
@@ -71,6 +72,7 @@ class _Fp8MLPFn(torch.autograd.Function):
         return y.view(*x.shape[:-1], n_out)
 
     @staticmethod
+    @once_differentiable   # (its outputs are written through addresses: no graph leads on)
     def backward(ctx, gy):
         x8, w18, h8, w28, z, s = ctx.saved_tensors
         sx, s1, sh, s2 = s.unbind()
