@@ -26,6 +26,11 @@ Entry points (same names as the C ABI in include/fp8ds.h):
     adamw_state_values(codes, exps, signed)          what 8-bit states stand for
 plus ScaleRing (a ring in a torch uint8 device tensor), BiasGradWorkspace and
 read_ring().
+
+stream: the torch stream to launch on, by default the current one.  Tensors that
+a call makes for another stream come from the current stream's memory, so that
+stream first waits for what the current one has queued; a call given all of its
+outputs (and workspace) does not wait.
 """
 import ctypes
 import os
@@ -166,6 +171,20 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _lend(stream, *made):
+    """Tensors a call made for its work on `stream` come from the current
+    stream's memory, which work queued there may still be using, and go back to
+    it: the given stream waits for that work, and the allocator for the given
+    stream."""
+    if stream is None:
+        return
+    here = torch.cuda.current_stream(made[0].device)
+    if stream != here:
+        stream.wait_stream(here)
+        for t in made:
+            t.record_stream(stream)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -225,6 +244,7 @@ class ScaleRing:
             raise Fp8dsError(f"hist_len {hist_len} outside [1, 1024]")
         self.hist_len, self.fmt = int(hist_len), int(fmt)
         self.buf = torch.empty(n, dtype=torch.uint8, device=device)
+        _lend(stream, self.buf)
         scale_ring_init(self.buf, hist_len, fmt, init_scale, stream)
         self._bufp = self.buf.data_ptr()
         self._sinv = lib().fp8_ring_scale_inv(self._bufp)
@@ -278,7 +298,10 @@ def fp8_quantize(x, fmt, ring, out=None, stream=None, max_blocks=None):
     """Quantize x (bf16, fp16 or fp32) with the ring's scale into uint8 codes;
     advances the ring."""
     in_type = _in_type(x)
-    out = torch.empty(x.shape, dtype=torch.uint8, device=x.device) if out is None else \
+    if out is None:
+        out = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+        _lend(stream, out)
+    else:
         _codes_out(out, x.numel(), x.device)
     rbuf = _ring_buf(ring)
     if max_blocks is not None:
@@ -307,6 +330,7 @@ def fp8_quantize_batch(xs, fmt, rings, outs=None, scale_inv_outs=None, stream=No
         raise Fp8dsError("fp8_quantize_batch: all tensors must share one dtype")
     if outs is None:
         outs = [torch.empty(x.shape, dtype=torch.uint8, device=x.device) for x in xs]
+        _lend(stream, *outs)
     if len(outs) != n:
         raise Fp8dsError("fp8_quantize_batch needs one output per tensor")
     for i in range(n):
@@ -332,12 +356,16 @@ def fp8_quantize_2d(x, fmt, ring, layout, out=None, out_t=None, stream=None):
     rows, cols = x.shape
     if layout not in (ROWWISE, TRANSPOSED, DUAL):
         raise Fp8dsError(f"layout {layout} is not ROWWISE, TRANSPOSED or DUAL")
+    given, given_t = out, out_t
     if layout in (ROWWISE, DUAL):
         out = torch.empty((rows, cols), dtype=torch.uint8, device=x.device) if out is None else \
             _need(out, "out", _U8, rows * cols)
     if layout in (TRANSPOSED, DUAL):
         out_t = torch.empty((cols, rows), dtype=torch.uint8, device=x.device) if out_t is None else \
             _need(out_t, "out_t", _U8, rows * cols)
+    made = [o for o, g in ((out, given), (out_t, given_t)) if o is not None and g is None]
+    if made:
+        _lend(stream, *made)
     _check(lib().fp8_quantize_2d(_ptr(x), rows, cols, in_type, int(fmt), int(layout), _ptr(_ring_buf(ring)),
                                  _ptr(out) if layout != TRANSPOSED else None,
                                  _ptr(out_t) if layout != ROWWISE else None, _stream(stream)))
@@ -348,7 +376,10 @@ def fp8_quantize_dynamic(x, fmt, ring, out=None, stream=None):
     """Dynamic scaling: quantize x with FMAX / amax(x); ring must have hist_len 1
     and afterwards holds scale_inv_used for the GEMM."""
     in_type = _in_type(x)
-    out = torch.empty(x.shape, dtype=torch.uint8, device=x.device) if out is None else \
+    if out is None:
+        out = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+        _lend(stream, out)
+    else:
         _codes_out(out, x.numel(), x.device)
     _check(lib().fp8_quantize_dynamic(_ptr(x), x.numel(), in_type, int(fmt), _ptr(_ring_buf(ring)), _ptr(out),
                                       _stream(stream)))
@@ -385,16 +416,21 @@ def fp8_bias_grad(g, rows=None, cols=None, fmt=None, g_scale_inv=None, out_f32=F
     esize = {G_E4M3: 1, G_E5M2: 1, G_F32: 4}.get(g_type, 2)
     _need(g, "g", (g.dtype,), int(rows) * int(cols) * esize, device=False)
     out_dtype = torch.float32 if out_f32 else torch.bfloat16
+    made = []
     if out is None:
         out = torch.empty(int(cols), dtype=out_dtype, device=g.device)
+        made.append(out)
     _need(out, "out", (out_dtype,), int(cols) * (4 if out_f32 else 2), device=False)
     if g_type in (G_E4M3, G_E5M2) and isinstance(g_scale_inv, torch.Tensor):
         _need(g_scale_inv, "g_scale_inv", _F32, 4, device=False)
     if workspace is None:
         workspace = BiasGradWorkspace(rows, cols, g.device)
+        made.append(workspace.buf)
     wbuf = workspace.buf if isinstance(workspace, BiasGradWorkspace) else workspace
     _need(wbuf, "workspace", _U8, bias_grad_workspace_bytes(rows, cols), device=False)
     _on_device(("g", g), ("out", out), ("g_scale_inv", g_scale_inv), ("workspace", wbuf))
+    if made:
+        _lend(stream, *made)
     _check(lib().fp8_bias_grad(_ptr(g), int(rows), int(cols), g_type, _addr(g_scale_inv), int(bool(out_f32)),
                                _ptr(out), _ptr(wbuf), _stream(stream)))
     return out
@@ -507,8 +543,11 @@ def fp8_mm(a, b, fmt_a, fmt_b, layout, m, n, k, a_scale_inv, b_scale_inv, bias=N
     tile forces a tile of the family (TILES name or index); max_workgroups
     bounds the grid so each workgroup runs several output tiles.
     """
+    given = out
     args, out = _mm_args(a, b, fmt_a, fmt_b, layout, m, n, k, a_scale_inv, b_scale_inv, bias, out, batch, lda,
                          ldb, ldc, stride_a, stride_b, stride_c, bias_fmt, bias_scale_inv)
+    if given is None:
+        _lend(stream, out)
     if tile is None and max_workgroups is None:
         _check(lib().fp8_mm(args, _stream(stream)))
     else:
@@ -524,6 +563,9 @@ def fp8_mm_pair(first, second, stream=None):
     b_scale_inv and optionally bias, out, ...).  Returns the two outputs."""
     a0, out0 = _mm_args(**first)
     a1, out1 = _mm_args(**second)
+    made = [o for o, d in ((out0, first), (out1, second)) if d.get("out") is None]
+    if made:
+        _lend(stream, *made)
     _check(lib().fp8_mm_pair(a0, a1, _stream(stream)))
     return out0, out1
 
@@ -540,6 +582,7 @@ def fp8_mm_epilogue(a, b, fmt_a, fmt_b, layout, m, n, k, a_scale_inv, b_scale_in
     preact received): bf16 device tensors [batch][m][ld_extra], by default laid
     out like the output (ldc, stride_c); residual may be `out` itself.  The
     other arguments are those of fp8_mm."""
+    given = out
     args, out = _mm_args(a, b, fmt_a, fmt_b, layout, m, n, k, a_scale_inv, b_scale_inv, bias, out, batch, lda,
                          ldb, ldc, stride_a, stride_b, stride_c, bias_fmt, bias_scale_inv)
     ldc = n if ldc is None else ldc
@@ -553,6 +596,8 @@ def fp8_mm_epilogue(a, b, fmt_a, fmt_b, layout, m, n, k, a_scale_inv, b_scale_in
                 _need(t, name, (torch.bfloat16,), nbytes)
     epi = _EPIARGS.pack(int(act), 0, _addr(residual), _addr(preact), _addr(grad_preact), ld, stride, ld, stride, ld,
                         stride)
+    if given is None:
+        _lend(stream, out)
     _check(lib().fp8_mm_epilogue(args, epi, _stream(stream)))
     return out
 

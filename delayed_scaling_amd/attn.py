@@ -15,7 +15,7 @@ import struct
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import _F32, IN_BF16, IN_F16, Fp8dsError, _check, _need, _stream, lib
+from . import _F32, IN_BF16, IN_F16, Fp8dsError, _check, _lend, _need, _stream, lib
 
 _ATTN_ARGS = struct.Struct("<32q4Q3q9if")    # fp8ds_attn_args, 352 bytes
 _WORKSPACE_AT = 264                          # its workspace field
@@ -109,10 +109,17 @@ def attn_forward(q, k, v, causal=False, window=0, scale=None, cu_seqlens_q=None,
     [Hq, rows]); a row that sees no key gets 0 and -infinity."""
     tail, shape = _tail(q, k, causal, window, scale, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k)
     dt, dev, qs, ks = q.dtype, q.device, q.shape, k.shape
-    out = torch.empty_like(q) if out is None else out
-    lse = q.new_empty(shape, dtype=torch.float32) if lse is None else _lse(lse, shape, dev)
+    made = []
+    if out is None:
+        made.append(out := torch.empty_like(q))
+    if lse is None:
+        made.append(lse := q.new_empty(shape, dtype=torch.float32))
+    else:
+        _lse(lse, shape, dev)
     args = _ATTN_ARGS.pack(*_view(q, "q", qs, dt, dev), *_view(k, "k", ks, dt, dev), *_view(v, "v", ks, dt, dev),
                            *_view(out, "out", qs, dt, dev), *_NO_GRADS, lse.data_ptr(), 0, *tail)
+    if made:
+        _lend(stream, *made)
     _check(lib().attn_forward(args, _stream(stream)))
     return out, lse
 
@@ -132,9 +139,13 @@ def attn_backward(dout, q, k, v, out, lse, causal=False, window=0, scale=None, c
     device tensor of at least attn_workspace_bytes, made per call if not given."""
     tail, shape = _tail(q, k, causal, window, scale, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k)
     dt, dev, qs, ks = q.dtype, q.device, q.shape, k.shape
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    made = []
+    if dq is None:
+        made.append(dq := torch.empty_like(q))
+    if dk is None:
+        made.append(dk := torch.empty_like(k))
+    if dv is None:
+        made.append(dv := torch.empty_like(v))
     lse = _lse(lse, shape, dev)
     args = _ATTN_ARGS.pack(*_view(q, "q", qs, dt, dev), *_view(k, "k", ks, dt, dev), *_view(v, "v", ks, dt, dev),
                            *_view(out, "out", qs, dt, dev), *_view(dout, "dout", qs, dt, dev),
@@ -142,10 +153,10 @@ def attn_backward(dout, q, k, v, out, lse, causal=False, window=0, scale=None, c
                            lse.data_ptr(), 0, *tail)
     nbytes = lib().attn_workspace_bytes(args)
     if workspace is None:
-        workspace = lse.new_empty(nbytes // 4)
-        if stream is not None:                # not handed out again before that stream is done with it
-            workspace.record_stream(stream)
+        made.append(workspace := lse.new_empty(nbytes // 4))
     _need(workspace, "workspace", _F32, nbytes)
+    if made:
+        _lend(stream, *made)
     args = args[:_WORKSPACE_AT] + workspace.data_ptr().to_bytes(8, "little") + args[_WORKSPACE_AT + 8:]
     _check(lib().attn_backward(args, _stream(stream)))
     return dq, dk, dv

@@ -12,7 +12,7 @@ import struct
 
 import torch
 
-from . import _IN_TYPE, _U8, Fp8dsError, _addr, _check, _need, _on_device, _stream, lib
+from . import _IN_TYPE, _U8, Fp8dsError, _addr, _check, _lend, _need, _on_device, _stream, lib
 
 ADAMW_BLOCK = 256                            # FP8DS_ADAMW_BLOCK
 _ADAM_TENSOR = struct.Struct("<7Qq")         # fp8ds_adamw_tensor, 64 bytes
@@ -123,10 +123,13 @@ def adamw_state_values(codes, exps, signed, out=None, stream=None):
     exp_avg, False for exp_avg_sq."""
     _need(codes, "codes", _U8, 0, device=False)
     _need(exps, "exps", _U8, state_exp_bytes(codes.numel()), device=False)
-    if out is None:
+    made = out is None
+    if made:
         out = torch.empty(codes.shape, dtype=torch.bfloat16, device=codes.device)
     _need(out, "out", (torch.bfloat16,), 2 * codes.numel(), device=False)
     _on_device(("codes", codes), ("exps", exps), ("out", out))
+    if made:
+        _lend(stream, out)
     _check(lib().adamw_state_values(_addr(codes), _addr(exps), codes.numel(), int(bool(signed)), _addr(out),
                                     _stream(stream)))
     return out
