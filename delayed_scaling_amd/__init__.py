@@ -393,9 +393,9 @@ def bias_grad_workspace_bytes(rows, cols):
 class BiasGradWorkspace:
     """Zero-filled device workspace for fp8_bias_grad on [rows, cols] gradients."""
 
-    def __init__(self, rows, cols, device="cuda"):
+    def __init__(self, rows, cols, device="cuda", least=16):
         self.shape = (int(rows), int(cols))
-        self.buf = torch.zeros(max(bias_grad_workspace_bytes(rows, cols), 16), dtype=torch.uint8, device=device)
+        self.buf = torch.zeros(max(bias_grad_workspace_bytes(rows, cols), int(least)), dtype=torch.uint8, device=device)
 
 
 def fp8_bias_grad(g, rows=None, cols=None, fmt=None, g_scale_inv=None, out_f32=False, out=None,

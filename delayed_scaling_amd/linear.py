@@ -27,23 +27,41 @@ from . import (_IN_TYPE, _MMARGS, _QJOB, BIAS_BF16, BIAS_F32, BIAS_NONE, E4M3, E
                BiasGradWorkspace, Fp8dsError, ScaleRing, _check, _stream, bias_grad_workspace_bytes, lib)
 
 
+class BiasWorkspaces:
+    """The bias-gradient workspaces of a layer, made larger as its shapes ask for
+    it (at least twice as large, so that those before add up to less).  None is
+    let go: a captured graph keeps the addresses it was captured with.  One made
+    within a capture is that graph's alone: its zeros are written by the replays."""
+
+    def __init__(self):
+        self.kept = []
+        self._shape = None
+
+    def get(self, rows, cols, device):
+        if self._shape == (rows, cols):
+            return self.kept[-1]
+        have = self.kept[-1].buf.numel() if self.kept else 0
+        if have < bias_grad_workspace_bytes(rows, cols):
+            new = BiasGradWorkspace(rows, cols, device, least=max(2 * have, 16))
+            if new.buf.is_cuda and torch.cuda.is_current_stream_capturing():
+                return new
+            self.kept.append(new)
+        self._shape = (rows, cols)
+        return self.kept[-1]
+
+
 class Fp8LinearState:
     """The three scale rings of one linear layer (x, w: E4M3; g: E5M2) and a
-    bias-gradient workspace, created on first use."""
+    bias-gradient workspaces, created on first use."""
 
     def __init__(self, hist_len=16, device="cuda"):
         self.ring_x = ScaleRing(hist_len, E4M3, device=device)
         self.ring_w = ScaleRing(hist_len, E4M3, device=device)
         self.ring_g = ScaleRing(hist_len, E5M2, device=device)
-        self.workspace = None
-        self._ws_shape = None
+        self.workspaces = BiasWorkspaces()
 
     def bias_workspace(self, rows, cols, device):
-        if self._ws_shape != (rows, cols):
-            if self.workspace is None or self.workspace.buf.numel() < bias_grad_workspace_bytes(rows, cols):
-                self.workspace = BiasGradWorkspace(rows, cols, device)
-            self._ws_shape = (rows, cols)
-        return self.workspace
+        return self.workspaces.get(rows, cols, device)
 
 
 def _input(t, name, dev):

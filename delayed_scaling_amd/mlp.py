@@ -14,10 +14,9 @@ of its own; the backward multiplies the forward's codes and dequantizes with the
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU, E4M3, E5M2, NN, NT, TN, BiasGradWorkspace,
-               Fp8dsError, ScaleRing, bias_grad_workspace_bytes, fp8_bias_grad, fp8_mm, fp8_mm_epilogue, fp8_mm_pair,
-               fp8_quantize, fp8_quantize_batch)
-from .linear import _input
+from . import (ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU, E4M3, E5M2, NN, NT, TN, Fp8dsError, ScaleRing,
+               fp8_bias_grad, fp8_mm, fp8_mm_epilogue, fp8_mm_pair, fp8_quantize, fp8_quantize_batch)
+from .linear import BiasWorkspaces, _input
 
 _ACTS = {"relu": ACT_RELU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH, "silu": ACT_SILU}
 
@@ -28,13 +27,11 @@ class Fp8MLPState:
     def __init__(self, hist_len=16, device="cuda"):
         self.x, self.w1, self.h, self.w2 = (ScaleRing(hist_len, E4M3, device=device) for _ in range(4))
         self.gy, self.gz = (ScaleRing(hist_len, E5M2, device=device) for _ in range(2))
-        self._workspace = None
+        self.workspaces = BiasWorkspaces()
 
     def workspace(self, rows, cols, device):
         """A bias-gradient workspace for [rows, cols] (all zero between calls)."""
-        if self._workspace is None or self._workspace.buf.numel() < bias_grad_workspace_bytes(rows, cols):
-            self._workspace = BiasGradWorkspace(rows, cols, device)
-        return self._workspace
+        return self.workspaces.get(rows, cols, device)
 
 
 class _Fp8MLPFn(torch.autograd.Function):
