@@ -186,6 +186,7 @@ class AdamW(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
+        at = -1                              # launches so far, over all groups: each rounds by bits of its own
         for group in self.param_groups:
             batches = {}
             for p in group["params"]:
@@ -194,7 +195,8 @@ class AdamW(torch.optim.Optimizer):
                 s = self.state[p] or self._init_state(p)
                 key = (p.device, p.dtype, p.grad.dtype, "master" in s, None if self.capturable else s["step"])
                 batches.setdefault(key, []).append(p)
-            for at, (key, ps) in enumerate(batches.items()):
+            for key, ps in batches.items():
+                at += 1
                 ss = [self.state[p] for p in ps]
                 if self.capturable:
                     torch._foreach_add_([s["step"] for s in ss], 1)

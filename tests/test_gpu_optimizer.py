@@ -172,3 +172,24 @@ def test_a_state_of_the_other_kind_resumes(capturable):
     torch.cuda.synchronize()
     close(mine, again, 4)
     assert all(int(opt2.state[p]["step"]) == 8 for p in again)
+
+
+@pytest.mark.parametrize("capturable", [False, True])
+def test_groups_round_by_bits_of_their_own(capturable):
+    """Equal tensors with equal gradients at the same place of two groups: the same
+    moments before rounding, rounded by different bits.  Of 4096 elements about a
+    third would differ if the bits were independent; equal bits differ nowhere."""
+    ds = require_gpu()
+    ps = [torch.nn.Parameter(torch.ones(4096, device="cuda")) for _ in range(3)]
+    opt = ds.AdamW([dict(params=ps[:1]), dict(params=ps[1:2], weight_decay=0.0), dict(params=ps[2:])], lr=LR,
+                   state_bits=8, capturable=capturable)
+    g = grads(0, [(4096,)])[0]
+    for _ in range(2):
+        for p in ps:
+            p.grad = g
+        opt.step()
+        torch.cuda.synchronize()
+        for key in ("exp_avg", "exp_avg_sq"):
+            for i in range(3):
+                a, b = opt.state[ps[i]][key], opt.state[ps[i - 1]][key]
+                assert (a != b).float().mean().item() > 0.05, (key, i)
