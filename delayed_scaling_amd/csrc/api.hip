@@ -247,7 +247,9 @@ int check_attn(const char* fn, const fp8ds_attn_args* a, bool backward, bool* em
   const bool packed = a->cu_seqlens_q != nullptr;
   if (packed != (a->cu_seqlens_k != nullptr))
     return set_error(FP8DS_EINVAL, "%s: cu_seqlens_q and cu_seqlens_k are given together", fn);
-  *empty = a->batch == 0 || a->heads_q == 0 || (a->max_q == 0 && (!backward || a->max_k == 0));
+  // (Without query rows or heads there are still dk and dv, which are zero.)
+  const bool queries = a->heads_q > 0 && a->max_q > 0, keys = a->heads_kv > 0 && a->max_k > 0;
+  *empty = a->batch == 0 || !(queries || (backward && keys));
   if (*empty) return FP8DS_OK;
   if (packed && (a->rows_q < 0 || a->rows_k < 0 || a->lse_stride_head < a->rows_q))
     return set_error(FP8DS_EINVAL, "%s: rows_q and rows_k must be >= 0, lse_stride_head at least rows_q", fn);
@@ -264,7 +266,7 @@ int check_attn(const char* fn, const fp8ds_attn_args* a, bool backward, bool* em
                          {"dk", &a->dk, a->heads_kv, a->max_k},    {"dv", &a->dv, a->heads_kv, a->max_k}};
   for (int i = 0; i < (backward ? 8 : 4); ++i) {
     const fp8ds_attn_view& v = *views[i].v;
-    if (views[i].rows == 0) continue;
+    if (views[i].rows == 0 || views[i].heads == 0) continue;
     if (!v.p) return set_error(FP8DS_EINVAL, "%s: %s is NULL", fn, views[i].name);
     if (!aligned16(v.p) || (v.stride_batch & 7) || (v.stride_row & 7) || (v.stride_head & 7))
       return set_error(FP8DS_EALIGN, "%s: %s is not 16-byte aligned, or a stride is not a multiple of 8", fn, views[i].name);
@@ -272,8 +274,8 @@ int check_attn(const char* fn, const fp8ds_attn_args* a, bool backward, bool* em
         v.stride_head > ((int64_t)1 << 40) || v.stride_batch > ((int64_t)1 << 50))
       return set_error(FP8DS_EINVAL, "%s: a stride of %s is out of range (stride_row in [head_dim, 2^24))", fn, views[i].name);
   }
-  if (a->max_q > 0 && !a->lse) return set_error(FP8DS_EINVAL, "%s: lse is NULL", fn);
-  if (backward && a->max_q > 0 && !a->workspace) return set_error(FP8DS_EINVAL, "%s: workspace is NULL", fn);
+  if (queries && !a->lse) return set_error(FP8DS_EINVAL, "%s: lse is NULL", fn);
+  if (backward && queries && !a->workspace) return set_error(FP8DS_EINVAL, "%s: workspace is NULL", fn);
   if ((reinterpret_cast<uintptr_t>(a->lse) & 3u) || (backward && !aligned16(a->workspace)) ||
       ((reinterpret_cast<uintptr_t>(a->cu_seqlens_q) | reinterpret_cast<uintptr_t>(a->cu_seqlens_k)) & 3u))
     return set_error(FP8DS_EALIGN, "%s: lse, workspace or cu_seqlens not aligned", fn);

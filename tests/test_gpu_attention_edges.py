@@ -44,3 +44,16 @@ def test_a_window_past_every_row_hides_nothing(window, tq, tk):
     torch.cuda.synchronize()
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
     assert all(torch.equal(a, b) for a, b in zip(got, ref)) and (ref[1] != 0).any() and (ref[2] != 0).any()
+
+
+@pytest.mark.parametrize("tq,hq", [(5, 0), (0, 4), (0, 0)])
+def test_no_query_leaves_zero_gradients(tq, hq):
+    """Without query heads or rows dk and dv are zero, not what their memory held."""
+    ds = require_gpu()
+    q, k = randn((2, tq, hq, 64), 330, "bf16"), randn((2, 70, 2, 64), 331, "bf16")
+    o, lse = ds.attn_forward(q, k, k)
+    out = [torch.full_like(k, 7.0) for _ in range(2)]
+    dq, dk, dv = ds.attn_backward(q, q, k, k, o, lse, dk=out[0], dv=out[1])
+    torch.cuda.synchronize()
+    assert o.shape == q.shape and lse.shape == (2, hq, tq) and dq.shape == q.shape
+    assert (dk == 0).all() and (dv == 0).all()
