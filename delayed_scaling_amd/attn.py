@@ -106,7 +106,8 @@ def attn_forward(q, k, v, causal=False, window=0, scale=None, cu_seqlens_q=None,
     the longest lengths).  causal aligns the last query with the last key;
     window w > 0 (with causal) lets a query see its last w keys only; scale
     defaults to D ** -0.5.  Returns (out like q, lse fp32 [B, Hq, Tq], packed
-    [Hq, rows]); a row that sees no key gets 0 and -infinity."""
+    [Hq, rows]); a row that sees no key gets 0 and -infinity.  Packed rows of no
+    sequence (before the first offset, past the last) are not written."""
     tail, shape = _tail(q, k, causal, window, scale, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k)
     dt, dev, qs, ks = q.dtype, q.device, q.shape, k.shape
     made = []
@@ -135,7 +136,8 @@ def attn_backward(dout, q, k, v, out, lse, causal=False, window=0, scale=None, c
                   max_seqlen_q=None, max_seqlen_k=None, dq=None, dk=None, dv=None, workspace=None, stream=None):
     """Gradients (dq, dk, dv) of attn_forward for the output's gradient dout,
     from its inputs, its outputs out and lse and the same options.  dq, dk, dv
-    may be given (slices of one dQKV tensor, say); workspace: a dense fp32
+    may be given (slices of one dQKV tensor, say); packed rows of no sequence
+    are not written; workspace: a dense fp32
     device tensor of at least attn_workspace_bytes, made per call if not given."""
     tail, shape = _tail(q, k, causal, window, scale, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k)
     dt, dev, qs, ks = q.dtype, q.device, q.shape, k.shape
@@ -165,7 +167,10 @@ def attn_backward(dout, q, k, v, out, lse, causal=False, window=0, scale=None, c
 class _AttentionFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, kw):
-        out, lse = attn_forward(q, k, v, **kw)
+        # Rows of no sequence are not written: zeros, for what comes after takes
+        # every row (an amax, a weight's gradient).
+        packed = kw["cu_seqlens_q"] is not None and isinstance(q, torch.Tensor)
+        out, lse = attn_forward(q, k, v, out=torch.zeros_like(q) if packed else None, **kw)
         ctx.save_for_backward(q, k, v, out, lse)
         ctx.kw = kw
         return out
@@ -177,12 +182,14 @@ class _AttentionFn(torch.autograd.Function):
         if dout.dtype != q.dtype or dout.stride(-1) != 1 or dout.data_ptr() % 16 or any(s % 8 for s in dout.stride()[:-1]):
             dout = dout.to(q.dtype).contiguous()
         dout = dout if dout.dim() < 3 or dout.shape[-3] < 2 or dout.stride(-3) >= dout.shape[-1] else dout.contiguous()
-        return (*attn_backward(dout, q, k, v, out, lse, **ctx.kw), None)
+        grads = [torch.zeros_like(t) for t in (q, k, v)] if ctx.kw["cu_seqlens_q"] is not None else (None,) * 3
+        return (*attn_backward(dout, q, k, v, out, lse, **ctx.kw, dq=grads[0], dk=grads[1], dv=grads[2]), None)
 
 
 def attention(q, k, v, causal=False, window=0, scale=None, cu_seqlens_q=None, cu_seqlens_k=None,
               max_seqlen_q=None, max_seqlen_k=None):
-    """attn_forward's out, differentiable in q, k and v."""
+    """attn_forward's out, differentiable in q, k and v.  Packed rows of no
+    sequence are zero, in out and in the gradients."""
     kw = dict(causal=causal, window=window, scale=scale, cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k,
               max_seqlen_q=max_seqlen_q, max_seqlen_k=max_seqlen_k)
     return _AttentionFn.apply(q, k, v, kw)

@@ -57,3 +57,23 @@ def test_no_query_leaves_zero_gradients(tq, hq):
     torch.cuda.synchronize()
     assert o.shape == q.shape and lse.shape == (2, hq, tq) and dq.shape == q.shape
     assert (dk == 0).all() and (dv == 0).all()
+
+
+def test_packed_rows_of_no_sequence_are_zero_in_autograd():
+    """A buffer longer than its sequences: the rest of the output and of the
+    gradients is zero, whatever the memory held (a next layer takes all rows)."""
+    ds = require_gpu()
+    rows, cu = 512, torch.tensor([7, 130, 130, 301], dtype=torch.int32, device="cuda")
+    leaf = [randn((rows, h, 64), 340 + i, "bf16").requires_grad_() for i, h in enumerate((4, 2, 2))]
+    do = randn((rows, 4, 64), 350, "bf16")
+    kw = dict(causal=True, cu_seqlens_q=cu, cu_seqlens_k=cu, max_seqlen_q=171, max_seqlen_k=171)
+    for h in (4, 2, 2, 4, 2, 2):                       # what the call's tensors may get
+        torch.full((rows, h, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+    y = ds.attention(*leaf, **kw)
+    y.backward(do)
+    o, lse = ds.attn_forward(*[x.detach() for x in leaf], **kw)
+    ref = ds.attn_backward(do, *[x.detach() for x in leaf], o, lse, **kw)
+    torch.cuda.synchronize()
+    for got, want in zip((y.detach(), *[x.grad for x in leaf]), (o, *ref)):
+        assert torch.equal(got[7:301], want[7:301])
+        assert (got[:7] == 0).all() and (got[301:] == 0).all()
