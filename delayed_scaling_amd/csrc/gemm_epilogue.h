@@ -112,8 +112,10 @@ __device__ __forceinline__ float act_slope(float z) {
     return __builtin_fmaf(0.3989422804014327f * z, e, z < 0.0f ? q : 1.0f - q);
   }
   if constexpr (ACT == kActGeluTanh) {
-    const float s = sigmoid(2.0f * kTanhA * z * __builtin_fmaf(kTanhB, z * z, 1.0f));
-    return __builtin_fmaf(z * s * (1.0f - s), 2.0f * kTanhA * __builtin_fmaf(3.0f * kTanhB, z * z, 1.0f), s);
+    // (s (1 - s) is zero long before z^2 would overflow; the two may not meet.)
+    const float zz = __builtin_fminf(z * z, 0x1p64f);
+    const float s = sigmoid(2.0f * kTanhA * z * __builtin_fmaf(kTanhB, zz, 1.0f));
+    return __builtin_fmaf(z * s * (1.0f - s), 2.0f * kTanhA * __builtin_fmaf(3.0f * kTanhB, zz, 1.0f), s);
   }
   if constexpr (ACT == kActSilu) {
     const float s = sigmoid(z);
