@@ -77,3 +77,60 @@ def test_packed_rows_of_no_sequence_are_zero_in_autograd():
     for got, want in zip((y.detach(), *[x.grad for x in leaf]), (o, *ref)):
         assert torch.equal(got[7:301], want[7:301])
         assert (got[:7] == 0).all() and (got[301:] == 0).all()
+
+
+def alone(ds, case, b, heads, hk, causal):
+    """Forward and backward of one key / value head's group by itself."""
+    q, k, v, do = (x[b:b + 1, :, s] for x, s in zip(case, (heads, slice(hk, hk + 1), slice(hk, hk + 1), heads)))
+    one = [x.contiguous() for x in (q, k, v, do)]
+    o, lse = ds.attn_forward(*one[:3], causal=causal)
+    return one, o, lse, ds.attn_backward(one[3], *one[:3], o, lse, causal=causal)
+
+
+@pytest.mark.parametrize("kind,b,hq,hkv,tq,tk,d", [
+    ("bf16", 3, 6, 3, 3662, 3662, 64),                 # 29 blocks of rows: the middle one has no partner
+    ("f16", 3, 6, 3, 3790, 3790, 128),                 # 30
+    ("bf16", 1, 16, 2, 4200, 3300, 128),               # 33; the first 900 rows see nothing
+    ("bf16", 5, 8, 1, 1700, 2500, 64)])                # 14
+def test_workgroups_of_two_row_blocks(kind, b, hq, hkv, tq, tk, d):
+    """Causal grids of more than 512 row blocks, whose workgroups take a block from
+    each end: out, lse and dQ of every head are the bits of its group alone (a grid
+    that is not paired), and two groups are checked in full against float64, dK and
+    dV too.  (dK and dV of a group alone are summed in other parts.)"""
+    ds = require_gpu()
+    blocks = -(-tq // 128)
+    assert b * hq * blocks > 512 and (hq // hkv) * blocks <= 512
+    say("attention in pairs", kind, b, hq, hkv, tq, tk, d)
+    case = [randn((b, t, h, d), 360 + i, kind) for i, (t, h) in enumerate(((tq, hq), (tk, hkv), (tk, hkv), (tq, hq)))]
+    q, k, v, do = case
+    o, lse = ds.attn_forward(q, k, v, causal=True)
+    dq, dk, dv = ds.attn_backward(do, q, k, v, o, lse, causal=True)
+    torch.cuda.synchronize()
+    rep = hq // hkv
+    same = lambda x, y: torch.equal(x.contiguous().view(torch.int16), y.contiguous().view(torch.int16))
+    for i in range(b):
+        for hk in range(hkv):
+            heads = slice(hk * rep, (hk + 1) * rep)
+            one, oo, ll, gg = alone(ds, case, i, heads, hk, True)
+            torch.cuda.synchronize()
+            assert same(o[i:i + 1, :, heads], oo) and torch.equal(lse[i:i + 1, heads], ll), (i, hk)
+            assert same(dq[i:i + 1, :, heads], gg[0]), (i, hk)
+    for i, hk in {(0, 0), (b - 1, hkv - 1)}:
+        say("  in full", i, hk)
+        heads = slice(hk * rep, (hk + 1) * rep)
+        pick = lambda x, s: x[i:i + 1, :, s]
+        check_dense((pick(q, heads), pick(k, slice(hk, hk + 1)), pick(v, slice(hk, hk + 1)), pick(do, heads)),
+                    pick(o, heads), lse[i:i + 1, heads],
+                    (pick(dq, heads), pick(dk, slice(hk, hk + 1)), pick(dv, slice(hk, hk + 1))), kind, True, 0, None)
+
+
+def test_long_rows_in_full():
+    """5000 causal rows of 128 columns, one head: every row of the output and of
+    the three gradients against float64."""
+    ds = require_gpu()
+    case = [randn((1, 5000, 1, 128), 380 + i, "bf16") for i in range(4)]
+    q, k, v, do = case
+    o, lse = ds.attn_forward(q, k, v, causal=True)
+    grads = ds.attn_backward(do, q, k, v, o, lse, causal=True)
+    torch.cuda.synchronize()
+    check_dense(case, o, lse, grads, "bf16", True, 0, None)
