@@ -60,12 +60,14 @@ constexpr float kNegInf = -__builtin_inff();
 // The backward pass carries P times 2^24 in bf16 (whose range is fp32's) and
 // takes the factor out of its sums: the hardware exponential flushes results
 // below 2^-126, and gradients of keys that every query all but ignores would
-// vanish there.  It costs nothing: the exponent rides on lse.  fp16 has no room
-// for it, and loses such values in its own rounding anyway.
+// vanish there.  It costs nothing: the exponent rides on lse.  fp16 ends at 2^16
+// and is coarse below 2^-14, so there P carries 2^15, which keeps it and dS = P
+// (dP - delta) of gradients down to 1e-9 off the coarse end (unlifted, dS of
+// 2e-7 was rounded to multiples of 6e-8); Fit below keeps large ones off the other.
 template <bool BF>
-constexpr float kLift = BF ? 24.0f : 0.0f;
+constexpr float kLift = BF ? 24.0f : 15.0f;
 template <bool BF>
-constexpr float kDrop = BF ? 0x1p-24f : 1.0f;
+constexpr float kDrop = BF ? 0x1p-24f : 0x1p-15f;
 constexpr uint32_t kOut = 0x80000000u;     // offset past every buffer: loads give zero
 
 template <int N>
@@ -198,6 +200,38 @@ __device__ __forceinline__ float dot8(v4i x, v4i y, float s) {
 __device__ __forceinline__ float max3(float x, float y, float z) {
   return __builtin_fmaxf(__builtin_fmaxf(x, y), z);
 }
+
+// fp16's end for dS: a factor (a power of two, one for the wave) under which every
+// value packed so far has stayed below 2^15.  It falls, and the sums formed under
+// the old one with it, when a value outgrows that: a test of the largest of 16 for
+// each block, and a product an element once it is not 1 (nine packed sequences of
+// 8192 tokens, forward and backward: 329 -> 337 us).  It goes to 16 times less than
+// it has to at most, so what is lost of a value is its own rounding or 2^-36 of
+// the largest.
+template <bool BF>
+struct Fit {
+  float f = 1.0f;
+  template <int N>
+  __device__ __forceinline__ void operator()(v16f& x, v16f (&sums)[N]) {
+    if constexpr (!BF) {
+      float top = __builtin_fabsf(x[0]);
+#pragma unroll
+      for (int r = 1; r < 15; r += 2) top = max3(top, __builtin_fabsf(x[r]), __builtin_fabsf(x[r + 1]));
+      top = __builtin_fmaxf(top, __builtin_fabsf(x[15])) * f;
+      // (An infinity stays one, in a row or column of its lane's that is lost to it.)
+      const bool finite = top < __builtin_inff();
+      if (__any(finite && top > 0x1p15f)) {
+        float shrink = 1.0f;
+        do shrink *= 0x1p-4f;
+        while (__any(finite && top * shrink > 0x1p15f));
+        f *= shrink;
+#pragma unroll
+        for (int i = 0; i < N; ++i) sums[i] *= shrink;
+      }
+      if (f != 1.0f) x *= f;
+    }
+  }
+};
 
 // The value of the lane 32 away.
 __device__ __forceinline__ float other_half(float x, bool hi) {
@@ -574,6 +608,7 @@ __global__ __launch_bounds__(64 * kWaves, FIX && DP == 128 ? 1 : 2) void attn_dq
     if (wrow >= s.nq) whi = 0;
     v16f dq[DP / 32] = {}, pk[FIX ? DP / 32 : 1] = {};
     float rest = 0.0f;                       // this lane's half of r, times 2^kLift
+    Fit<BF> fit;
 
     int clo, chi;                            // keys every query of this wave sees
     {
@@ -615,6 +650,7 @@ __global__ __launch_bounds__(64 * kWaves, FIX && DP == 128 ? 1 : 2) void attn_dq
         }
 #pragma unroll
         for (int r = 0; r < 16; ++r) rest += st[r];
+        fit(st, dq);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           v4i x, p;
@@ -638,6 +674,10 @@ __global__ __launch_bounds__(64 * kWaves, FIX && DP == 128 ? 1 : 2) void attn_dq
     }
     rest = (rest + other_half(rest, h)) * kDrop<BF>;
     if (row < s.nq && h == 0) a.delta[stat] = delta + rest;
+    if constexpr (!BF) {
+#pragma unroll
+      for (int i = 0; i < DP / 32; ++i) dq[i] *= 1.0f / fit.f;
+    }
     if constexpr (FIX) {
 #pragma unroll
       for (int i = 0; i < DP / 32; ++i) dq[i] -= rest * pk[i];
@@ -778,6 +818,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_dkv_kernel(AttnArgs a) {
   };
 
   v16f dk[kBlocks] = {}, dv[kBlocks] = {};
+  Fit<BF> fit;
   if (total > 0) {
     issue();
     issue();
@@ -862,6 +903,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_dkv_kernel(AttnArgs a) {
           x[r] = see ? x[r] : 0.0f;
         }
       }
+      fit(x, dk);
       auto pack8 = [&](const v16f& y, int k) __attribute__((always_inline)) {
         return v4i{pack2<BF>(y[8 * k], y[8 * k + 1]), pack2<BF>(y[8 * k + 2], y[8 * k + 3]),
                    pack2<BF>(y[8 * k + 4], y[8 * k + 5]), pack2<BF>(y[8 * k + 6], y[8 * k + 7])};
@@ -909,6 +951,10 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_dkv_kernel(AttnArgs a) {
       r0 += kTile;
       if (r0 == t1 * kTile) r0 = t0 * kTile;
     }
+  }
+  if constexpr (!BF) {
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i) dk[i] *= 1.0f / fit.f;
   }
   if (a.parts > 1) {
     const int blocks = a.blocks / a.parts;

@@ -1,27 +1,29 @@
 """Attention where a kernel's own structure could let it go wrong: row maxima late
 in a tile, masks at the ends of the integers, long causal grids whose workgroups
 take two row blocks.  References and tolerances as in test_gpu_attention."""
+import numpy as np
 import pytest
 import torch
 
 from gpu_util import require_gpu, say
-from test_gpu_attention import check_dense, randn
+from oracle import attention as at
+from test_gpu_attention import check, check_dense, f64, randn
 
 pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("kind", ["f16", "bf16"])
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("at", [64, 96, 97, 99, 104, 127])
-def test_a_maximum_in_the_middle_of_an_unmasked_tile(kind, d, at):
+@pytest.mark.parametrize("where", [64, 96, 97, 99, 104, 127])
+def test_a_maximum_in_the_middle_of_an_unmasked_tile(kind, d, where):
     """One key of the second tile outweighs the keys before it by e^30 = 2^43 (fp16
     ends at 2^16): every row's maximum has to have seen it, whichever register of
     the scores it is in."""
     ds = require_gpu()
-    say("attention maximum", kind, d, at)
+    say("attention maximum", kind, d, where)
     q, k, v, do = (randn((1, 192, 2, d), 300 + i, kind, 0.1 if i < 2 else 1.0) for i in range(4))
     q += 1
-    k[0, at] = 30 / d ** 0.5
+    k[0, where] = 30 / d ** 0.5
     o, lse = ds.attn_forward(q, k, v)
     grads = ds.attn_backward(do, q, k, v, o, lse)
     torch.cuda.synchronize()
@@ -134,3 +136,56 @@ def test_long_rows_in_full():
     grads = ds.attn_backward(do, q, k, v, o, lse, causal=True)
     torch.cuda.synchronize()
     check_dense(case, o, lse, grads, "bf16", True, 0, None)
+
+
+@pytest.mark.parametrize("big", ["k", "q"])
+@pytest.mark.parametrize("sigma", [1e-5, 1e-4, 300.0, 5000.0])
+@pytest.mark.parametrize("tq,hq,d,causal", [(1500, 4, 64, True), (700, 1, 128, True), (300, 2, 64, False)])
+def test_fp16_gradients_small_and_large(monkeypatch, big, sigma, tq, hq, d, causal):
+    """Score gradients of 1e-9 to 1e5, past both ends of fp16.  Inside, P and dS are
+    carried times 2^15, or less where that would leave the type: they lose their
+    rounding (2^-11) and, of dS, at most 2^-36 of the largest; the outputs lose what
+    fp16 loses at their size.  Keys large beside queries (or the other way round)
+    bring dQ (dK) into fp16's normal range, or keep it from the upper end."""
+    ds = require_gpu()
+    say("attention fp16", big, sigma, tq, hq, d, causal)
+    up = 2.0 ** 8 if sigma < 1 else 2.0 ** -6
+    q, k, v, do = (randn((1, tq, h, d), 400 + i, "f16") for i, h in enumerate((hq, 1, 1, hq)))
+    q, k = (q / up, k * up) if big == "k" else (q * up, k / up)
+    do = (do.float() * sigma).half()
+    o, lse = ds.attn_forward(q, k, v, causal=causal)
+    grads = ds.attn_backward(do, q, k, v, o, lse, causal=causal)
+    torch.cuda.synchronize()
+    qn, kn, vn, gn = (f64(x)[0] for x in (q, k, v, do))
+    see = at.visible(tq, tq, causal, 0)
+    sums = [0.0] * 4
+    for h in range(hq):
+        args = qn[:, h], kn[:, 0], vn[:, 0]
+        _, _, p, _ = at.forward(*args, d ** -0.5, see)
+        top = np.abs(p * (gn[:, h] @ vn[:, 0].T - (gn[:, h] * (p @ vn[:, 0])).sum(1, keepdims=True))).max()
+        monkeypatch.setitem(at.TINY, "f16", 2.0 ** -40 + 2.0 ** -36 * top)
+        r = at.backward(gn[:, h], *args, d ** -0.5, see)
+        t = at.backward_tolerance(gn[:, h], *args, d ** -0.5, see, "f16")
+        if big == "k":
+            check(f64(grads[0])[0, :, h], r[0], t[0] + 2.0 ** -25, (h, "dq"))
+        sums = [a + b for a, b in zip(sums, (r[1], r[2], t[1], t[2]))]
+    if big == "q":
+        check(f64(grads[1])[0, :, 0], sums[0], sums[2] + 2.0 ** -25, "dk")
+    if sigma < 1000:
+        check(f64(grads[2])[0, :, 0], sums[1], sums[3] + 2.0 ** -25, "dv")
+
+
+def test_an_infinite_fp16_gradient_stays_in_its_row():
+    """A gradient that overflowed in one row reaches that row's dQ and the keys it
+    sees; keys after it (in the same tile) keep their bits, and so do other rows."""
+    ds = require_gpu()
+    q, k, v, do = (randn((1, 200, 1, 64), 420 + i, "f16") for i in range(4))
+    o, lse = ds.attn_forward(q, k, v, causal=True)
+    ref = ds.attn_backward(do, q, k, v, o, lse, causal=True)
+    do2 = do.clone()
+    do2[0, 70, 0, 5] = float("inf")
+    got = ds.attn_backward(do2, q, k, v, o, lse, causal=True)
+    torch.cuda.synchronize()
+    rows = [i for i in range(200) if i != 70]
+    assert torch.equal(got[0][0, rows], ref[0][0, rows]) and not torch.isfinite(got[0][0, 70]).any()
+    assert not torch.isfinite(got[1][0, :71]).any() and torch.equal(got[1][0, 71:], ref[1][0, 71:])
