@@ -216,6 +216,8 @@ class AdamW(torch.optim.Optimizer):
                                grad_scale=grad_scale,
                                exp_avg_exp=[s["exp_avg_exp"] for s in ss] if eight else None,
                                exp_avg_sq_exp=[s["exp_avg_sq_exp"] for s in ss] if eight else None, seed=seed)
+                # (The kernel writes through addresses; a graph that saved a parameter has to know.)
+                torch.autograd.graph.increment_version(ps)
         return loss
 
 

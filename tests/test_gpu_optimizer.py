@@ -193,3 +193,21 @@ def test_groups_round_by_bits_of_their_own(capturable):
             for i in range(3):
                 a, b = opt.state[ps[i]][key], opt.state[ps[i - 1]][key]
                 assert (a != b).float().mean().item() > 0.05, (key, i)
+
+
+def test_a_graph_from_before_the_step_raises():
+    """A backward pass through parameters that the step has changed since raises, as
+    after torch's optimizers, instead of mixing old and new values."""
+    ds = require_gpu()
+    p = torch.nn.Parameter(torch.ones(64, device="cuda"))
+    opt = ds.AdamW([p], lr=LR)
+    loss = (p * p).sum()
+    loss.backward(retain_graph=True)
+    opt.step()
+    with pytest.raises(RuntimeError, match="inplace operation"):
+        loss.backward()
+    opt.zero_grad()
+    (p * p).sum().backward()
+    opt.step()
+    torch.cuda.synchronize()
+    assert torch.isfinite(p).all() and (p < 1).all()
