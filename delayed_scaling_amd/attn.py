@@ -164,6 +164,15 @@ def attn_backward(dout, q, k, v, out, lse, causal=False, window=0, scale=None, c
     return dq, dk, dv
 
 
+def _fits(t, dtype):
+    """Whether a gradient that autograd hands over can be read where it stands: the
+    library's conditions on a view (a new tensor meets them, a contiguous one
+    need not: it can begin anywhere)."""
+    st, n = t.stride(), t.shape
+    return (t.dtype is dtype and st[-1] == 1 and t.data_ptr() % 16 == 0
+            and not any(s % 8 for s, k in zip(st[:-1], n) if k > 1) and (n[-3] < 2 or n[-1] <= st[-3] < 1 << 24))
+
+
 class _AttentionFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, kw):
@@ -179,9 +188,8 @@ class _AttentionFn(torch.autograd.Function):
     @once_differentiable   # (its outputs are written through addresses: no graph leads on)
     def backward(ctx, dout):
         q, k, v, out, lse = ctx.saved_tensors
-        if dout.dtype != q.dtype or dout.stride(-1) != 1 or dout.data_ptr() % 16 or any(s % 8 for s in dout.stride()[:-1]):
-            dout = dout.to(q.dtype).contiguous()
-        dout = dout if dout.dim() < 3 or dout.shape[-3] < 2 or dout.stride(-3) >= dout.shape[-1] else dout.contiguous()
+        if not _fits(dout, q.dtype):
+            dout = torch.empty(dout.shape, dtype=q.dtype, device=q.device).copy_(dout)
         grads = [torch.zeros_like(t) for t in (q, k, v)] if ctx.kw["cu_seqlens_q"] is not None else (None,) * 3
         return (*attn_backward(dout, q, k, v, out, lse, **ctx.kw, dq=grads[0], dk=grads[1], dv=grads[2]), None)
 

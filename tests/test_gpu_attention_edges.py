@@ -189,3 +189,20 @@ def test_an_infinite_fp16_gradient_stays_in_its_row():
     rows = [i for i in range(200) if i != 70]
     assert torch.equal(got[0][0, rows], ref[0][0, rows]) and not torch.isfinite(got[0][0, 70]).any()
     assert not torch.isfinite(got[1][0, :71]).any() and torch.equal(got[1][0, 71:], ref[1][0, 71:])
+
+
+@pytest.mark.parametrize("make", [
+    lambda x: torch.cat([x.reshape(-1)[:1], x.reshape(-1)])[1:].view(x.shape),        # contiguous, off 16 bytes
+    lambda x: x.transpose(1, 2).contiguous().transpose(1, 2),
+    lambda x: torch.nn.functional.pad(x, (0, 4))[..., :64]])
+def test_gradients_in_any_layout(make):
+    """The autograd function takes the output's gradient wherever it stands."""
+    ds = require_gpu()
+    leaf = [randn((2, 60, h, 64), 430 + i, "bf16").requires_grad_() for i, h in enumerate((4, 2, 2))]
+    do = randn((2, 60, 4, 64), 440, "bf16")
+    o, lse = ds.attn_forward(*[x.detach() for x in leaf], causal=True)
+    ref = ds.attn_backward(do, *[x.detach() for x in leaf], o, lse, causal=True)
+    y = ds.attention(*leaf, causal=True)
+    got = torch.autograd.grad(y, leaf, make(do))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, ref))
