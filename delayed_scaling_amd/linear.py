@@ -64,14 +64,22 @@ class Fp8LinearState:
         return self.workspaces.get(rows, cols, device)
 
 
+def _dense(t):
+    """t, or a copy of it if it is not contiguous from a 16-byte aligned address
+    (contiguous() does not move one that begins elsewhere)."""
+    if t.is_contiguous() and t.data_ptr() % 16 == 0:
+        return t
+    return torch.empty(t.shape, dtype=t.dtype, device=t.device).copy_(t)
+
+
 def _input(t, name, dev):
     """A caller's tensor going to a kernel: bf16 / fp16 / fp32, on the GPU of
-    the layer, made contiguous."""
+    the layer, made dense."""
     if t.dtype not in _IN_TYPE:
         raise Fp8dsError(f"{name} must be bf16, fp16 or fp32, not {t.dtype}")
     if t.device != dev:
         raise Fp8dsError(f"{name} is on {t.device}; the layer runs on {dev}")
-    return t if t.is_contiguous() else t.contiguous()
+    return _dense(t)
 
 
 def _mm(a, b, c, fmt_a, layout, m, n, k, sa, sb, bias=None, bias_kind=BIAS_NONE):
@@ -124,7 +132,7 @@ class _Fp8LinearFn(torch.autograd.Function):
             bias_kind = {torch.bfloat16: BIAS_BF16, torch.float32: BIAS_F32}.get(b.dtype)
             if bias_kind is None or b.device != dev or b.numel() != n_out:
                 raise Fp8dsError("bias must be a bf16 or fp32 tensor of out_features elements on the layer's GPU")
-            b = b if b.is_contiguous() else b.contiguous()
+            b = _dense(b)
         y = torch.empty((t, n_out), dtype=torch.bfloat16, device=dev)
         _check(L.fp8_mm(_mm(x8, w8, y.data_ptr(), E4M3, NT, t, n_out, n_in, sp, sp + 4, b, bias_kind), st))
         ctx.save_for_backward(saved)
@@ -145,8 +153,7 @@ class _Fp8LinearFn(torch.autograd.Function):
         x8 = saved.data_ptr()
         w8, sp = x8 + wo, x8 + so
         g2 = gy.reshape(-1, n_out)
-        if g2.dtype != torch.bfloat16 or not g2.is_contiguous():
-            g2 = g2.to(torch.bfloat16).contiguous()
+        g2 = _dense(g2 if g2.dtype == torch.bfloat16 else g2.to(torch.bfloat16))
         L, st = lib(), _stream(None)
         g8t = torch.empty((t, n_out), dtype=torch.uint8, device=dev)
         g8 = g8t.data_ptr()

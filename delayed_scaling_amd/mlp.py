@@ -16,7 +16,7 @@ from torch.autograd.function import once_differentiable
 
 from . import (ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU, E4M3, E5M2, NN, NT, TN, Fp8dsError, ScaleRing,
                fp8_bias_grad, fp8_mm, fp8_mm_epilogue, fp8_mm_pair, fp8_quantize, fp8_quantize_batch)
-from .linear import BiasWorkspaces, _input
+from .linear import BiasWorkspaces, _dense, _input
 
 _ACTS = {"relu": ACT_RELU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH, "silu": ACT_SILU}
 
@@ -76,7 +76,7 @@ class _Fp8MLPFn(torch.autograd.Function):
         state, (t, hid), n_in, n_out, dev = ctx.state, z.shape, x8.shape[1], w28.shape[0], z.device
         bf = torch.bfloat16
         need_x, need_w1, need_b1, need_w2, need_b2, need_r = ctx.needs_input_grad[:6]
-        g2 = gy.reshape(t, n_out).to(bf).contiguous()
+        g2 = _dense(gy.reshape(t, n_out).to(bf))
         g8 = fp8_quantize(g2, E5M2, state.gy)
         dx = dw1 = db1 = dw2 = db2 = None
         if need_w2:
