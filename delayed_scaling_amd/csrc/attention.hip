@@ -384,8 +384,8 @@ __device__ __forceinline__ void key_range(const AttnArgs& a, const Seq& s, int r
 // instructions and its LDS reads as its 32 products keep the matrix unit busy,
 // and the two waves' shares overlap only in part (MFMA busy 49 % of SIMD
 // cycles, no LDS conflicts, 85 MB from HBM at 2 x 4096).  Measured, causal bf16:
-// 8192 tokens, 16 heads of 128 on 4: 271-285 us = 0.96-1.01 PFLOP/s; 2 x 4096,
-// 16 heads on 8: 150-160 us; 4 x 512, 16 heads of 64: 12 us.
+// 8192 tokens, 16 heads of 128 on 4: 267-287 us = 0.96-1.03 PFLOP/s; 2 x 4096,
+// 16 heads on 8: 150-169 us; 4 x 512, 16 heads of 64: 12-13 us.
 template <int DP, bool BF>
 __global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_kernel(AttnArgs a) {
   constexpr int kTileBytes = kTile * DP * 2;
@@ -525,9 +525,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_kernel(AttnArgs a) {
 
 // ---------------------------------------------------------------------------
 // Backward: dQ (and delta, which the dK / dV kernel after it reads).  Bound as
-// the forward is, with three products a tile for its two (MFMA busy 53 %).
-// Measured, causal bf16: 2 x 4096, 16 heads of 128 on 8: 222-230 us = 0.90-0.93
-// PFLOP/s; 4 x 512, 16 heads of 64: 18-19 us.
+// the forward is, with three products a tile for its two (MFMA busy 50 %); at
+// head_dim 128 without FIX addresses of the output go to memory before the loop
+// and come back after it (92 bytes a lane: 12 MB at 2 x 4096).  Measured, causal bf16: 2 x 4096, 16 heads of 128 on 8:
+// 220-245 us = 0.84-0.94 PFLOP/s; 4 x 512, 16 heads of 64: 18-19 us.
 //
 // delta from the rounded O carries O's rounding.  The rows of dS should sum to
 // zero, so the sum r_i of those formed with delta' is the error of delta', and
@@ -700,7 +701,7 @@ __global__ __launch_bounds__(64 * kWaves, FIX && DP == 128 ? 1 : 2) void attn_dq
 // buffers keep tiles n and n + 1 readable while n + 2 arrives, so one barrier
 // a tile is enough.  Bound by that one wave's issue (MFMA busy 47 % of SIMD
 // cycles, LDS reads 29 % of CU cycles without conflicts).  Measured, causal
-// bf16: 2 x 4096, 16 heads of 128 on 8: 310-330 us = 0.83-0.89 PFLOP/s (478
+// bf16: 2 x 4096, 16 heads of 128 on 8: 309-352 us = 0.78-0.89 PFLOP/s (478
 // before the pipelining); 4 x 512, 16 heads of 64: 20-21 us.
 //
 // Few keys, or few key / value heads, make fewer workgroups than keep the
@@ -710,8 +711,8 @@ __global__ __launch_bounds__(64 * kWaves, FIX && DP == 128 ? 1 : 2) void attn_dq
 // the order of the parts, and rounds once.  Measured (causal bf16, dQ and dK / dV
 // together, alone and shared): 1 x 8192, 16 heads of 128 on 4: 1257 and 913 us;
 // 1 x 2048: 297 and 133; 1 x 1024, 8 heads of 64 on 1: 203 and 48.  Nine packed
-// sequences of 8192 tokens in all (16 heads of 128 on 4, window 1024): 170 us, or
-// 143 and 18 for the join.
+// fp16 sequences of 8192 tokens in all (16 heads of 128 on 4, window 1024): 170 us,
+// or 143 and 18 for the join (148 since Fit).
 //
 // Where one part's sums of a wave's 32 keys stand: which = 0 dK, 1 dV.  Packed
 // sequences: sequence b's blocks are numbered from k0 / 128 + b on, so no two

@@ -371,10 +371,15 @@ int fp8_mm_pair_tile(const fp8_mm_args* first, const fp8_mm_args* second);
  * [batch][heads_q][max_q].  Packed (cu_seqlens_q and cu_seqlens_k not NULL):
  * device int32[batch + 1] row offsets of the sequences, laid end to end in the
  * row dimension (batch strides unused); no sequence may be longer than max_q /
- * max_k (rows past that are not computed); lse is [heads_q][lse_stride_head].
+ * max_k (rows past that, and rows of no sequence, are not written); lse is
+ * [heads_q][lse_stride_head].
  * No value outside a sequence's rows is read for it.  A NaN or infinity in a
  * row of v that a causal or window mask hides from some queries only may reach
- * the others within 64 rows of the mask's edge.
+ * the others within 64 rows of the mask's edge; the same holds for k and dq, and
+ * for rows of q and dout with dk and dv.
+ * Products take P and, in the backward pass, dS = P (dP - delta) rounded to the
+ * operands' type, under a power of two that keeps small ones off the type's
+ * coarse end (fp16: large ones below its end, too); sums are fp32.
  * head_dim: a multiple of 8 up to 128.  Nothing is allocated; results do not
  * depend on scheduling (no atomic sums).  Outputs must not overlap inputs. */
 typedef struct fp8ds_attn_view {
@@ -399,7 +404,7 @@ typedef struct fp8ds_attn_args {
 int attn_forward(const fp8ds_attn_args* args, void* stream);
 /* dq, dk, dv from dout, the forward's inputs and its out and lse.  The
  * workspace depends on the shapes alone (no pointer but cu_seqlens_q's being
- * there is looked at): 8 bytes a row of lse, and up to 135 MB of partial sums
+ * there is looked at): 8 bytes a row of lse, and up to 90 MB of partial sums
  * where dk and dv have too few rows to fill the device by themselves. */
 size_t attn_workspace_bytes(const fp8ds_attn_args* args);
 int attn_backward(const fp8ds_attn_args* args, void* stream);
